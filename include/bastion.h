@@ -479,7 +479,10 @@ bastion_status bastion_tree_attn_q8(const void *q, const void *k_tree, const voi
 /*
  * bastion_tree_attn_shared -- bastion_tree_attn for a batch that shares a
  * prefix (prefix, prefix_len as for bastion_tree_attn_q8, both required), with
- * caches of the inputs' type.  Everything else is as for bastion_tree_attn_q8.
+ * caches of the inputs' type.  Everything else is as for bastion_tree_attn_q8;
+ * dtype bf16: softmax weights in bf16, held to at most 2^8 (sums stay finite
+ * while keys x the largest |value| is below 2^120; a part of a result below
+ * 2^-100 may be lost).
  */
 size_t bastion_tree_attn_shared_workspace_size(bastion_dtype dtype, int B, int n_max, int Hq, int Hkv, int d,
                                                const bastion_kv_cache *kv, const bastion_kv_cache *prefix);

@@ -19,8 +19,8 @@
 //   * Row maxima would cost reductions across lanes, so none is taken per tile:
 //     scores are held against a row's reference (a maximum of earlier
 //     tiles), and only where some score exceeds it by more than 2^TH, which a
-//     vote of the tile's threads finds, are new maxima reduced and O rescaled.
-//     The result does not depend on the reference.
+//     vote of the tile's threads finds, are new references reduced, 2^HEAD above
+//     the maximum, and O rescaled.  The result does not depend on the reference.
 //
 // 8-bit tiles.  K's and V's codes enter the MMA as they are (kind::f8f6f4);
 // Q and P are split into two 8-bit parts so that no accuracy is lost beside the
@@ -310,11 +310,17 @@ template <int D, bool Q8, int RM>
 struct CtxSoftmax {
   using LY = CtxLayout<D, Q8, RM>;
   // How far a score (with its V scale) may exceed its row's reference (log2)
-  // before the reference is raised: bf16 weights and fp32 sums have room for 2^96; the 8-bit parts do
-  // not (SHIFT + TH = 11: the largest weight is then 2^11).  A larger TH means
-  // fewer changes, a larger SHIFT finer small weights; rows of token sizes e^(N/2)
-  // (the listed cases') exceed TH = 4 in a quarter of a range's tiles, 7 in an eighth.
-  static constexpr float TH = Q8 ? 7.f : 96.f;
+  // before the reference is raised, and how far above the row's largest score it is
+  // then set.  A larger sum of the two means fewer changes.  bf16 weights are exact
+  // to their eight bits at any size, so HEAD costs nothing but the last 2^16 of the
+  // fp32 range downwards; a weight is at most 2^8, as in the attention over
+  // bf16 caches alone, and O stays finite while keys x |V| is below 2^120
+  // (16 trees behind 16381 shared keys: 231 us; HEAD 8 238, HEAD 0 305).
+  // The 8-bit parts have no such room (SHIFT + TH = 11: the largest weight is then
+  // 2^11).  A larger SHIFT means finer small weights; where the sizes of keys vary
+  // as e^(N/2), TH = 4 is exceeded in a quarter of a range's tiles, 7 in an eighth.
+  static constexpr float TH = Q8 ? 7.f : 8.f;
+  static constexpr float HEAD = Q8 ? 0.f : 16.f;
   static constexpr int SHIFT = 4;
 
   // The piece's rows of Q into shared memory: bf16 for bf16 tiles, two e4m3
@@ -619,7 +625,7 @@ struct CtxSoftmax {
           for (int i = 4; i < C; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
           return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         };
-        // bf16: the largest raw score against the lowest reference, which with 2^96 of
+        // bf16: the largest raw score against the lowest reference, which with 2^24 of
         // room settles nearly every tile (8-bit, with 2^7: no gain measured); then
         // row by row.  (In chunks, as all passes: half the scores in registers took
         // 456 and 229 us where all at once took 459 and 232, with the spills.)
@@ -697,11 +703,11 @@ struct CtxSoftmax {
           float up, mn;
           if (unset) {
             const float top = unordered(o);
-            mn = isnan(top) ? 0.f : fmaxf(mo, top);   // (a NaN is a seen key; its row stays NaN)
+            mn = isnan(top) ? 0.f : fmaxf(mo, top + HEAD);   // (a NaN is a seen key; its row stays NaN)
             up = mn - mo;
             if (mn == CT_UNSET && table[key] >= 0) bars->unset[grp] = 1;
           } else {
-            up = o == ORDERED_LOWEST ? 0.f : ceilf(unordered(o));
+            up = o == ORDERED_LOWEST ? 0.f : ceilf(unordered(o)) + HEAD;
             mn = mo + up;
           }
           mref[key] = mn;
