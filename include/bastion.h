@@ -451,13 +451,14 @@ bastion_status bastion_kv_read_q8(const bastion_kv_cache_q8 *kv, bastion_dtype d
  * not written; a row that sees no key is zero.  What cache entries beyond
  * ctx_len[b] or prefix_len and tree rows j >= n[b] hold does not matter; the
  * K/V of a node j < n[b] must be finite, also for rows that do not see it.
- * dtype bf16: tensor cores; the codes enter them as they are, Q and the
- * softmax weights as sums of two 8-bit parts (error of a weight at most 2^-7
- * relative or 2^-13 of its row's largest weight, whichever is more, and less
- * than the weight itself; weights that meet values of very different sizes are
- * held by their product with the value's scale, and a key whose part of the result
- * is below 2^-50 of the context's largest value, or 2^-110, may be left out);
- * accumulation in fp32.  dtype f32: fp32 throughout.
+ * dtype bf16: tensor cores; the codes enter them as they are, Q as the sum of
+ * two e4m3 parts (an element is exact from 2^-6.8 of its row's largest on and
+ * off by at most 2^-14 of that below), the softmax weights, times their keys' V
+ * scales, as the sum of three e5m2 parts (off by at most 2^-8.8 relative or 2^-24
+ * of the row's largest such product, whichever is more; a bf16 weight is off by
+ * up to 2^-8; a key whose part of the result is below 2^-50 of the context's
+ * largest value, or 2^-110, may be left out); the weights of the tree's own nodes
+ * are bf16; accumulation in fp32.  dtype f32: fp32 throughout.
  * Requires d in {64, 128}, Hq % Hkv == 0 (any ratio), Hq <= 1024, n_max <= 256,
  * B <= 512, page sizes 8, 16, 32, 64 or 128, 16-byte aligned tensors.
  * ws: at least bastion_tree_attn_q8_workspace_size() bytes (never 0 for sizes

@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 
 from tree_speculative_decoding_bastion_gb300 import binding as bn  # noqa: E402
 
-from .context_cases import Case  # noqa: E402
+from .context_cases import Case, scale_exponents  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -21,8 +21,8 @@ def built():
 
 
 @pytest.mark.parametrize("where", ["own", "prefix"])
-@pytest.mark.parametrize("rows", [1, 8, 13, 40])
-@pytest.mark.parametrize("gap,v_exp", [(90, 40), (24.5, 100), (8.5, 105), (7.5, 105)])
+@pytest.mark.parametrize("rows", [1, 20, 70])
+@pytest.mark.parametrize("gap,v_exp", [(90, 40), (24.5, 100), (8.5, 105)])
 def test_a_late_key_of_a_large_value(where, rows, gap, v_exp):
     """bf16 caches: in every head a key `gap` binades above all others, late in some
     CTA's range, whose value is 2^v_exp.  The result is that value."""
@@ -52,3 +52,119 @@ def test_a_late_key_of_a_large_value(where, rows, gap, v_exp):
     assert int(c.err) == 0
     c.check()
     assert float(c.out[0, 0].min()) > 2.0 ** (v_exp - 8)
+
+
+def tight(c, contexts=None):
+    """(want, bound) of a Case over an 8-bit cache with bf16 inputs.  Besides the output's
+    half step and the scores' error (context_cases): a weight that meets codes is an f16
+    (2^-11 relative) in three e5m2 parts (2^-9 of it, or 2^-24 of its row's largest
+    weight, both times the keys' V scales; test_context_parts_cpu), 1.25 2^-9 together;
+    one that meets a tree's value is a bf16 (2^-8)."""
+    want = torch.full(c.q.shape, float("nan"), dtype=torch.float64, device="cuda")
+    bound = torch.zeros_like(want)
+    g, d = c.Hq // c.Hkv, c.d
+    for b, parts in enumerate(contexts or c.contexts()):
+        m = c.n[b]
+        ctx = sum(k.shape[1] for k, _ in parts)
+        see = torch.ones(m, ctx + m, dtype=torch.bool)
+        for i in range(m):
+            for j in range(m):
+                see[i, ctx + j] = bool((int(c.words[b, i, j // 64]) >> (j % 64)) & 1)
+        see = see.cuda()
+        for h in range(c.Hkv):
+            keys = torch.cat([k[h] for k, _ in parts] + [c.kt[b, :m, h].double()])
+            vals = torch.cat([v[h] for _, v in parts] + [c.vt[b, :m, h].double()])
+            x = c.q[b, :m, h * g:(h + 1) * g].double()
+            z = (torch.einsum("igd,jd->igj", x, keys) * c.scale).masked_fill(~see[:, None], float("-inf"))
+            wt = torch.softmax(z, -1)
+            ev = scale_exponents(vals)
+            ev[ctx:] = ev[ctx:].max()
+            peak = (wt * 2.0 ** (ev + 1)).amax(-1, keepdim=True)   # (a row's scale may be one more than its values need)
+            werr = wt * 2.0 ** -8
+            werr[..., :ctx] = torch.maximum(wt * 1.25 * 2.0 ** -9, peak * 1.01 * 2.0 ** -24 / 2.0 ** ev)[..., :ctx]
+            amax = x.abs().amax(-1, keepdim=True)
+            dz = x.norm(dim=-1)[..., None] * keys.norm(dim=-1) * c.scale * ((d + 4) * 2.0 ** -24)
+            # elements of q below 2^-6.8 of their row's largest are off by up to 2^-14 of it
+            small = (x.abs() < amax * 2.0 ** -6.8).double()
+            dz = dz + torch.einsum("igd,jd->igj", small, keys.abs()) * amax * 2.0 ** -14 * c.scale
+            # an error dz of the scores moves a weight and the sum that divides it
+            move = 2.0 * dz.amax(-1, keepdim=True) + 2.0 ** -18
+            o = torch.einsum("igj,jd->igd", wt, vals)
+            want[b, :m, h * g:(h + 1) * g] = o
+            bound[b, :m, h * g:(h + 1) * g] = (torch.einsum("igj,jd->igd", werr + wt * move, vals.abs())
+                                               + o.abs() * (2.0 ** -8 * 1.01 + move))
+    return want, bound
+
+
+def check_tight(c, contexts=None, floor=0.0):
+    want, bound = tight(c, contexts)
+    idle = torch.isnan(want)
+    got = c.out.double()
+    assert bool((got[idle] == 5.0).all()), "rows behind the last node were written"
+    off = (got - want).abs() - bound - floor
+    bad = ~idle & ~(off <= 0)
+    if bool(bad.any()):
+        i = tuple(int(v) for v in bad.nonzero()[0])
+        raise AssertionError(f"{int(bad.sum())} of {int((~idle).sum())} elements off, first {i}: got {float(got[i])}, "
+                             f"want {float(want[i])}, bound {float(bound[i])}")
+
+
+def flat_context(c, scores, values):
+    """Request 0's own 8-bit context: key j scores scores[j] (nats, in every row and KV head;
+    held by the first element), all its values are values[j]; tree nodes score and hold 0."""
+    L, t = c.own.lens[0], c.own.t
+    t["k"][0, :, :L] = 0
+    t["ks"][0, :, :L] = 127
+    t["vs"][0, :, :L] = 127
+    c.q[0] = 0.0
+    c.q[0, ..., 0] = 1.0 / 16.0 / c.scale                    # a code of 16 x scores a nat
+    code = lambda x: torch.as_tensor(x, dtype=torch.float32).to(torch.float8_e4m3fn).view(torch.uint8).cuda()  # noqa: E731
+    t["k"][0, :, :L, 0] = code(scores * 16.0)
+    t["v"][0, :, :L] = code(values)[:, None]
+    for x, name in ((c.own.k64, "k"), (c.own.v64, "v")):
+        x[0] = t[name][0, :, :L].view(torch.float8_e4m3fn).double()
+    c.kt[:] = 0.0
+    c.vt[:] = 0.0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [2, 15, 25, 40])
+@pytest.mark.parametrize("gap", [8, 10])
+def test_a_flat_tail_behind_a_sink(gap, rows, d):
+    """Equal keys of e^-gap of the sink's weight each, most of them in the same CTA's range:
+    their rounding has one sign and adds up."""
+    L, Hkv = 6000, 96
+    c = Case(61, [rows], rows, 2 * Hkv, Hkv, d, "bf16", True, 0, [L], None, spread=0.0)
+    scores, values = np.zeros(L), np.ones(L)
+    scores[::1000], values[::1000] = gap, -1.0               # (of the head's ranges each has one)
+    flat_context(c, scores, values)
+    c.call()
+    torch.cuda.synchronize()
+    check_tight(c)
+
+
+@pytest.mark.parametrize("rows", [2, 25, 40])
+def test_tails_of_every_size_behind_a_sink(rows):
+    """Scores spread over 12 nats below the sink, values that cancel in the mean."""
+    L, Hkv = 8000, 64
+    c = Case(62, [rows], rows, 2 * Hkv, Hkv, 128, "bf16", True, 0, [L], None, spread=0.0)
+    r = np.random.default_rng(62)
+    scores, values = r.uniform(0, 8, L), np.where(r.random(L) < 0.5, 1.0, -0.9375)
+    scores[::2000], values[::2000] = 12.0, 0.5
+    flat_context(c, scores, values)
+    c.call()
+    torch.cuda.synchronize()
+    check_tight(c)
+
+
+@pytest.mark.parametrize("form", ["q8", "q8_prefix"])
+@pytest.mark.parametrize("spread", [0.0, 1.0, 2.0])
+@pytest.mark.parametrize("rows,Hq,Hkv,d,page", [(1, 8, 2, 128, 16), (5, 8, 2, 64, 0), (13, 8, 2, 128, 0), (30, 8, 2, 64, 8),
+                                                (64, 8, 2, 128, 16)])
+def test_weights_keep_more_bits_than_the_output(rows, Hq, Hkv, d, page, spread, form):
+    c = Case(63, [rows, max(1, rows - 3)], rows, Hq, Hkv, d, "bf16", True, page, [1500, 333],
+             None if form == "q8" else 700, page, spread=spread, room=3)
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    check_tight(c)

@@ -23,8 +23,8 @@
 //     the maximum, and O rescaled.  The result does not depend on the reference.
 //
 // 8-bit tiles.  K's and V's codes enter the MMA as they are (kind::f8f6f4);
-// Q and P are split into two 8-bit parts so that no accuracy is lost beside the
-// cache's own rounding:
+// Q and P are split into 8-bit parts, so that what they lose stays below what the
+// bf16 output loses:
 //   Q 2^-e = hi + lo, both e4m3, e the row's scale exponent (q8.cuh) or at most
 //     3 more: a bf16 has eight significant bits, hi takes the upper four
 //     (rounded), the signed remainder fits the four of lo -- the sum is exact for
@@ -32,18 +32,23 @@
 //     2^-14 of the amax, below.
 //   The weights that meet the codes are those times their key's V scale, u =
 //     2^(score + ev); a row's reference is a maximum of score + ev, so u is held
-//     against the row's largest u.  u 2^4 = hi + lo, hi e5m2 (range: 2^-16 .. 2^11;
-//     the row's largest lies at 2^3 at least, so a key is lost only below 2^-20 of
-//     it), lo e4m3: off by at most 2^-7 relative or 2^-10 absolute (2^-13 of the
-//     row's largest); about 2^-9.5 in the mean square, less than the output's bf16
-//     rounding.
+//     against the row's largest u.  u 2^8 = hi + mid + lo, all e5m2, by way of f16: hi
+//     and mid are cut off after three significant bits of what is left, lo is
+//     rounded to its three.  Of an f16's eleven bits two at most are then lost: off
+//     by at most 2^-9 relative, with the f16's rounding 2^-8.8 (a bf16 2^-8), 2^-11
+//     in the mean square and of either sign.  The smallest step of an e5m2 is 2^-16 and the row's
+//     largest weight lies at 2^7 at least (up to 2^15): a weight below 2^-15 of the
+//     largest is off by up to 2^-24 of it instead.  (With two parts, e5m2 and
+//     e4m3, a weight below 2^-12 of the largest had three bits: 20000 equal keys
+//     behind a sink came out off by 3%.)
 // The tree's own keys and values are bf16 and use kind::f16 with the bf16 Q,
 // on the same accumulators.
 //
 // Roles: warps 0-15 softmax (warp w: keys 32 (w mod 4) .. + 31, the lanes of
 // its TMEM quarter; row group w / 4), warp 16 TMA producer of K, warp 19 of V,
 // warp 17 MMA issuer, warp 18 the records of attn_work.cuh.
-// S^T passes through two TMEM buffers, P through two shared-memory buffers, K and
+// S^T passes through two TMEM buffers, P through two in shared memory (128 rows with
+// an 8-bit cache: one), K and
 // V through a ring of slots (of a tile of the cache's type, 128 x d codes or
 // bf16; in an 8-bit cache's ring a bf16 tree tile takes two) in the order in which
 // the MMAs take them, K0 K1 V0 K2 V1 ..: a freed slot is filled at once, where in
@@ -53,9 +58,9 @@
 // tiles, K(0) is its item 0, K(i) item 2 i - 1, V(i) item 2 i + 2, the last V item
 // 2 m - 1.
 // Measured: a CTA begins its first tile 5 us after launch (the partition 2, Q, the
-// first references); then an 8-bit tile of 128 rows takes 4.3 thousand cycles, bound by the
-// softmax's instructions (issue slots 56% busy, tensor pipe 26%: 4 trees of 128
-// over 32768 keys 461 us), a bf16 one 2.4 thousand (16 trees behind 16381 shared
+// first references); then an 8-bit tile of 128 rows takes 4.9 thousand cycles, bound by the
+// softmax's instructions (4 trees of 128 over 32768 keys
+// 520 us), a bf16 one 2.4 thousand (16 trees behind 16381 shared
 // keys 230 us), an 8-bit tile of few rows 1.9 thousand, bound by latency (16 tokens
 // over 512 to 8192 keys 44 us, 3.6 TB/s).
 // Every mbarrier wait is bounded in time; after an expiry the CTA issues no
@@ -112,18 +117,25 @@ struct CtxLayout {
   static constexpr int WIDE = Q8 ? 2 : 1;               // slots of a bf16 tile
   static constexpr int QB = RM * D * 2;                 // Q in bf16
   static constexpr int Q8B = RM == 64 ? 128 * 128 : QB; // ... in two 8-bit parts
-  // One P buffer: 128 keys x RM rows, bf16 or two 8-bit parts, which lie RM rows of
-  // 8 bits apart: 64 rows side by side in the keys' 128-byte lines, else in two tiles
-  static constexpr int PBUF = CA_KEYS * RM * 2;
-  static constexpr int P_LO = RM == 64 ? 64 : PBUF / 2;
+  // P in tiles of 128 keys x 128 bytes.  bf16: a tile of 64 rows.  8-bit: 128 rows of a
+  // part, or 64 of two side by side.  Without an 8-bit cache two buffers.  With one,
+  // three tiles: of 128 rows the three parts of one buffer (the pass that tests a
+  // tile's scores comes before any weight is written, and P V of the tile before is
+  // done by then); of up to 64 rows, whose streams are independent, two buffers of
+  // hi and mid, and a tile of both buffers' lo.
+  static constexpr int PT = CA_KEYS * 128;
+  static constexpr int P_TILES = Q8 ? 3 : RM / 32;
+  static BST_DEV int p_buffer(bool two, int pb) { return Q8 ? (two ? pb * PT : 0) : pb * (RM / 64) * PT; }
+  static BST_DEV int p_mid(bool two) { return two ? 64 : PT; }                       // from hi
+  static BST_DEV int p_lo(bool two, int pb) { return two ? (2 - pb) * PT + pb * 64 : 2 * PT; }
   static constexpr int Q16_OFF = 0;
   static constexpr int Q8_OFF = QB;
   static constexpr int RING_OFF = Q8 ? QB + Q8B : QB;
-  // what 227 KB leave: head_dim 128: 6 slots with an 8-bit cache, 4 without (64 rows: 10 and 5)
-  static constexpr int ROOM = (227 * 1024 - RING_OFF - 2 * PBUF - 3 * 1024) / SLOT;
+  // what 227 KB leave: head_dim 128: 6 slots with an 8-bit cache, 4 without (64 rows: 8 and 5)
+  static constexpr int ROOM = (227 * 1024 - RING_OFF - P_TILES * PT - 3 * 1024) / SLOT;
   static constexpr int SLOTS = (ROOM < CT_MAX_SLOTS ? ROOM : CT_MAX_SLOTS) / WIDE * WIDE;
   static constexpr int P_OFF = RING_OFF + SLOTS * SLOT;
-  static constexpr int MREF_OFF = P_OFF + 2 * PBUF;  // float[128] references
+  static constexpr int MREF_OFF = P_OFF + P_TILES * PT;  // float[128] references
   static constexpr int QSC_OFF = MREF_OFF + 512;        // float[128] (8-bit cache) row scale of the 8-bit Q times scale log2(e)
   // int[128] maxima as ordered integers, lowest between uses; then the rises of
   // the references, at the end the rows' factors (floats)
@@ -135,7 +147,8 @@ struct CtxLayout {
   static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
   static_assert(sizeof(CtxBars) <= 512, "barriers");
   static_assert(USED <= 227 * 1024, "exceeds the shared memory of one CTA");
-  static_assert(SLOTS >= 4 && SLOTS % WIDE == 0, "ring");
+  // (at least three tiles of the larger kind: the producers' waits by parity, see `take`)
+  static_assert(SLOTS >= 3 * WIDE && SLOTS % WIDE == 0, "ring");
 };
 
 // One lane of a converged warp.
@@ -260,19 +273,24 @@ BST_DEV uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// A pair of weights as hi (e5m2) and lo (e4m3) codes, 16 bits of each.  By way
-// of f16, whose eleven bits are more than the parts hold together and whose
-// upper byte an e5m2 is: five instructions a pair.
-BST_DEV void split_weights(float2 v, uint32_t &hi, uint32_t &lo) {
-  uint32_t h, back, rest;
-  uint16_t a, b;
+// A pair of weights as f16, whose upper byte is the e5m2 that it is cut off to.
+BST_DEV uint32_t weight_pair(float2 v) {
+  uint32_t h;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v.y), "f"(v.x));
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
-  hi = a;
-  back = __byte_perm(hi, 0, 0x1404);
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(back));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(rest));
-  lo = b;
+  return h;
+}
+// The upper bytes of two pairs (four codes), and what a pair has left without them (exact).
+BST_DEV uint32_t upper_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
+BST_DEV uint32_t without_upper(uint32_t h) {
+  uint32_t rest;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(h & 0xff00ff00u));
+  return rest;
+}
+// A pair rounded to e5m2 codes (16 bits).
+BST_DEV uint32_t e5m2_pair(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
 }
 // A pair of scaled query elements (at most 448) as e4m3 codes hi and lo.
 BST_DEV void split_query(float2 v, uint32_t &hi, uint32_t &lo) {
@@ -316,12 +334,12 @@ struct CtxSoftmax {
   // fp32 range downwards; a weight is at most 2^8, as in the attention over
   // bf16 caches alone, and O stays finite while keys x |V| is below 2^120
   // (16 trees behind 16381 shared keys: 231 us; HEAD 8 238, HEAD 0 305).
-  // The 8-bit parts have no such room (SHIFT + TH = 11: the largest weight is then
-  // 2^11).  A larger SHIFT means finer small weights; where the sizes of keys vary
+  // The 8-bit parts have no such room (SHIFT + TH = 15: the largest weight is then
+  // 2^15, an f16).  A larger SHIFT means finer small weights; where the sizes of keys vary
   // as e^(N/2), TH = 4 is exceeded in a quarter of a range's tiles, 7 in an eighth.
   static constexpr float TH = Q8 ? 7.f : 8.f;
   static constexpr float HEAD = Q8 ? 0.f : 16.f;
-  static constexpr int SHIFT = 4;
+  static constexpr int SHIFT = 8;
 
   // The piece's rows of Q into shared memory: bf16 for bf16 tiles, two e4m3
   // parts and the row scale for 8-bit ones.
@@ -759,7 +777,11 @@ struct CtxSoftmax {
       }
       // ---- P^T: 2^x, the row sums, and the parts for the second MMA
       const int pb = idx & 1;
-      uint8_t *P = smem + LY::P_OFF + pb * LY::PBUF;
+      uint8_t *P = smem + LY::P_OFF + LY::p_buffer(TWO, pb);
+      if (Q8 && !TWO && t != t_first) {        // one buffer: P V of the tile before has read it
+        mbar_wait(&bars->pv_done[(idx - 1) & 1], ((idx - 1) >> 1) & 1, abort, CT_WAIT_NS);
+        __syncwarp();
+      }
       const float wj = !Q8 ? 1.f : kx.valid ? pow2i(kx.ev - E + SHIFT) : 0.f;   // 2^(dev + SHIFT)
       const float2 w2 = make_float2(wj, wj);
 #pragma unroll
@@ -776,33 +798,41 @@ struct CtxSoftmax {
           }
         }
         const int rc = (r0 + c) >> 3;        // index of the 8-row chunk
-        uint32_t hi[C / 2], lo[C / 2];       // pairs: bf16, or 16 bits of each 8-bit part
+        uint32_t w[C / 2];                   // pairs: bf16, or f16
 #pragma unroll
         for (int e = 0; e < C / 2; ++e) {
           float2 v = make_float2(ex2f(x[2 * e]), ex2f(x[2 * e + 1]));
           l[c / 2 + e] = __fadd2_rn(l[c / 2 + e], v);
           if constexpr (Q8) v = __fmul2_rn(v, w2);
           if constexpr (F8)
-            split_weights(v, hi[e], lo[e]);
+            w[e] = weight_pair(v);
           else
-            hi[e] = bf16x2(v.x, v.y);
+            w[e] = bf16x2(v.x, v.y);
         }
         if constexpr (F8) {
-          uint8_t *at = P + key * 128 + (((rc >> 1) ^ (key & 7)) << 4);
-          uint8_t *at_lo = RM == 64 ? P + key * 128 + ((((rc >> 1) + 4) ^ (key & 7)) << 4) : at + LY::P_LO;
-          if constexpr (C == 16) {
-            *reinterpret_cast<uint4 *>(at) = make_uint4(two16(hi[0], hi[1]), two16(hi[2], hi[3]), two16(hi[4], hi[5]), two16(hi[6], hi[7]));
-            *reinterpret_cast<uint4 *>(at_lo) =
-                make_uint4(two16(lo[0], lo[1]), two16(lo[2], lo[3]), two16(lo[4], lo[5]), two16(lo[6], lo[7]));
-          } else {
-            *reinterpret_cast<uint2 *>(at + (rc & 1) * 8) = make_uint2(two16(hi[0], hi[1]), two16(hi[2], hi[3]));
-            *reinterpret_cast<uint2 *>(at_lo + (rc & 1) * 8) = make_uint2(two16(lo[0], lo[1]), two16(lo[2], lo[3]));
-          }
+          // into the 16-byte chunk of the rows in the key's line
+          auto put = [&](int tile, int chunk, auto four) {
+            uint8_t *at = P + tile + key * 128 + ((((rc >> 1) + chunk) ^ (key & 7)) << 4);
+            if constexpr (C == 16)
+              *reinterpret_cast<uint4 *>(at) = make_uint4(four(0), four(2), four(4), four(6));
+            else
+              *reinterpret_cast<uint2 *>(at + (rc & 1) * 8) = make_uint2(four(0), four(2));
+          };
+          auto upper = [&](int e) { return upper_bytes(w[e], w[e + 1]); };
+          auto cut = [&] {
+#pragma unroll
+            for (int e = 0; e < C / 2; ++e) w[e] = without_upper(w[e]);
+          };
+          put(0, 0, upper);
+          cut();
+          put(TWO ? 0 : LY::PT, TWO ? 4 : 0, upper);
+          cut();
+          put(TWO ? (2 - pb) * LY::PT : 2 * LY::PT, TWO ? 4 * pb : 0, [&](int e) { return two16(e5m2_pair(w[e]), e5m2_pair(w[e + 1])); });
         } else {
 #pragma unroll
           for (int k = 0; k < C / 8; ++k)
-            *reinterpret_cast<uint4 *>(P + ((rc + k) >> 3) * (LY::PBUF / 2) + key * 128 + ((((rc + k) & 7) ^ (key & 7)) << 4)) =
-                make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+            *reinterpret_cast<uint4 *>(P + ((rc + k) >> 3) * LY::PT + key * 128 + ((((rc + k) & 7) ^ (key & 7)) << 4)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
       }
       // ---- values behind the last key must not reach the MMA (0 x NaN).  It takes
@@ -1152,7 +1182,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1) ctx_attn_kernel(const __grid_co
           __syncwarp();
           tc_fence_after();
           const uint32_t vaddr = smem_u32(smem + LY::RING_OFF + st * LY::SLOT);
-          const uint64_t pd = sdesc_sw128(smem_u32(smem + LY::P_OFF + pb * LY::PBUF), LY::PBUF / 2, 1024);
+          const uint64_t pd = sdesc_sw128(smem_u32(smem + LY::P_OFF + LY::p_buffer(two, pb)), LY::PT, 1024);
           // (fewer than 128 columns: even and odd tiles have an O each)
           const uint32_t dO = tb + CT_SBUF * 128 + (two ? pb * 64 : 0);
           const uint32_t first = t < t0 + (two ? 2 : 1) ? 0u : 1u;
@@ -1162,19 +1192,23 @@ __global__ void __launch_bounds__(CT_THREADS, 1) ctx_attn_kernel(const __grid_co
           // half of the 128 rows, the others repeat what lies behind and are not read
           if (f8) {
             const uint64_t vd = D == 128 ? sdesc_sw128(vaddr, 16384, 1024) : sdesc_sw64(vaddr, 8192, 512);
-            const uint32_t id_hi = ctx_idesc(0, 1, 1, 1, N), id_lo = ctx_idesc(0, 0, 1, 1, N);
-            const uint32_t lo = LY::P_LO;
+            const uint32_t id = ctx_idesc(0, 1, 1, 1, N);
+            const uint32_t mid = LY::p_mid(two), lo = LY::p_lo(two, pb);
             if (keys > CA_KEYS - 32) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((kk * 4096) >> 4), id_hi, kk ? 1u : first);
+                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((kk * 4096) >> 4), id, kk ? 1u : first);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((lo + kk * 4096) >> 4), id_lo, 1u);
+                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((mid + kk * 4096) >> 4), id, 1u);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((lo + kk * 4096) >> 4), id, 1u);
             } else {
               for (int kk = 0; kk * 32 < keys; ++kk) {
-                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((kk * 4096) >> 4), id_hi, kk ? 1u : first);
-                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((lo + kk * 4096) >> 4), id_lo, 1u);
+                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((kk * 4096) >> 4), id, kk ? 1u : first);
+                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((mid + kk * 4096) >> 4), id, 1u);
+                mma_if(leader, true, dO, vd + ((kk * 32 * D) >> 4), pd + ((lo + kk * 4096) >> 4), id, 1u);
               }
             }
           } else {
