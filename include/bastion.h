@@ -456,9 +456,10 @@ bastion_status bastion_kv_read_q8(const bastion_kv_cache_q8 *kv, bastion_dtype d
  * off by at most 2^-14 of that below), the softmax weights, times their keys' V
  * scales, as the sum of three e5m2 parts (off by at most 2^-8.8 relative or 2^-24
  * of the row's largest such product, whichever is more; a bf16 weight is off by
- * up to 2^-8; a key whose part of the result is below 2^-50 of the context's
- * largest value, or 2^-110, may be left out); the weights of the tree's own nodes
- * are bf16; accumulation in fp32.  dtype f32: fp32 throughout.
+ * up to 2^-8); the weights of the tree's own nodes are bf16; accumulation in
+ * fp32.  Values may have any size from 2^-90 to 2^100, also side by side: a part
+ * of a result below 2^-70 of the largest |value| among the request's keys, or
+ * below 2^-100, may be lost.  dtype f32: fp32 throughout.
  * Requires d in {64, 128}, Hq % Hkv == 0 (any ratio), Hq <= 1024, n_max <= 256,
  * B <= 512, page sizes 8, 16, 32, 64 or 128, 16-byte aligned tensors.
  * ws: at least bastion_tree_attn_q8_workspace_size() bytes (never 0 for sizes

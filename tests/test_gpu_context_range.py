@@ -80,8 +80,9 @@ def tight(c, contexts=None):
             ev = scale_exponents(vals)
             ev[ctx:] = ev[ctx:].max()
             peak = (wt * 2.0 ** (ev + 1)).amax(-1, keepdim=True)   # (a row's scale may be one more than its values need)
-            werr = wt * 2.0 ** -8
-            werr[..., :ctx] = torch.maximum(wt * 1.25 * 2.0 ** -9, peak * 1.01 * 2.0 ** -24 / 2.0 ** ev)[..., :ctx]
+            step = peak * 1.01 * 2.0 ** -24 / 2.0 ** ev
+            werr = torch.maximum(wt * 2.0 ** -8, torch.minimum(wt, step))
+            werr[..., :ctx] = torch.maximum(wt * 1.25 * 2.0 ** -9, step)[..., :ctx]
             amax = x.abs().amax(-1, keepdim=True)
             dz = x.norm(dim=-1)[..., None] * keys.norm(dim=-1) * c.scale * ((d + 4) * 2.0 ** -24)
             # elements of q below 2^-6.8 of their row's largest are off by up to 2^-14 of it
@@ -168,3 +169,78 @@ def test_weights_keep_more_bits_than_the_output(rows, Hq, Hkv, d, page, spread, 
     torch.cuda.synchronize()
     assert int(c.err) == 0
     check_tight(c)
+
+
+def rescale(c, cache, e):
+    """V rows of a Case's 8-bit cache: exponents e (int64 [B, Hkv, L], -127 .. 127) for the scales
+    that they have; a row of exponent -127 becomes zero."""
+    e = torch.as_tensor(e).cuda()
+    zero = e == -127
+    L = e.shape[2]
+    cache.t["vs"][:, :, :L] = (e + 127).to(torch.uint8)
+    cache.t["v"][:, :, :L] = torch.where(zero[..., None], torch.zeros_like(cache.t["v"][:, :, :L]), cache.t["v"][:, :, :L])
+    for b, n in enumerate(cache.lens):
+        rows = cache.t["v"][b, :, :n].view(torch.float8_e4m3fn).double() * torch.exp2(e[b, :, :n].double())[..., None]
+        cache.v64[b] = rows
+
+
+def largest(c):
+    return max(float(v.abs().max()) for parts in c.contexts() for _, v in parts if v.numel())
+
+
+@pytest.mark.parametrize("rows", [1, 12, 40])
+@pytest.mark.parametrize("e", [-90, 40, 64, 67, 90, 110])
+def test_zero_values_before_large_ones(e, rows):
+    """The first 32 (and the first 140) keys of every 512 hold zeros under the smallest scale."""
+    c = Case(64, [rows], rows, 8, 2, 128, "bf16", True, 0, [3000], None)
+    at = torch.arange(3000)
+    ev = torch.full((1, 2, 3000), e, dtype=torch.int64)
+    ev[0, 0, at % 512 < 32] = -127
+    ev[0, 1, at % 512 < 140] = -127
+    rescale(c, c.own, ev)
+    c.vt[:] = 0.0
+    c.call()
+    torch.cuda.synchronize()
+    check_tight(c)
+
+
+@pytest.mark.parametrize("rows", [1, 12, 40])
+@pytest.mark.parametrize("lo,hi", [(-60, 60), (-126, 110), (0, 100), (-120, -20)])
+def test_value_scales_that_differ_within_a_context(lo, hi, rows):
+    c = Case(65, [rows, 1], rows, 8, 2, 128, "bf16", True, 0, [1900, 300], 700, 0, spread=0.5)
+    r = np.random.default_rng(65)
+    for cache in (c.own, c.pre):
+        rescale(c, cache, r.integers(lo, hi + 1, (len(cache.lens), 2, max(cache.lens))))
+    c.call()
+    torch.cuda.synchronize()
+    check_tight(c, floor=largest(c) * 2.0 ** -70)
+
+
+@pytest.mark.parametrize("rows", [1, 12, 40])
+@pytest.mark.parametrize("v_exp,tree_exp", [(-90, -90), (-90, 0), (90, 90), (0, -90), (0, 90), (90, -60), (-50, 60)])
+def test_values_of_contexts_and_trees_of_every_size(v_exp, tree_exp, rows):
+    c = Case(66, [rows, 2], max(rows, 2), 8, 2, 64, "bf16", True, 16, [1900, 0], 300, 16, v_exp=v_exp)
+    c.vt *= 2.0 ** tree_exp
+    c.call()
+    torch.cuda.synchronize()
+    check_tight(c, floor=max(largest(c), float(torch.nan_to_num(c.vt.double()).abs().max())) * 2.0 ** -70)
+
+
+@pytest.mark.parametrize("ctx", [100, 3000])
+def test_a_dominating_key_of_a_tiny_value(ctx):
+    """A key far above the others whose value is 2^140 times smaller than theirs: the row is
+    that value, off by no more than may be left out."""
+    c = Case(67, [2], 2, 4, 2, 128, "bf16", True, 0, [ctx], None)
+    e = torch.randint(5, 20, (1, 2, ctx), generator=torch.Generator().manual_seed(67))
+    e[:, :, 50] = -120
+    rescale(c, c.own, e)
+    t = c.own.t
+    t["k"][0, :, 50] = 0
+    t["k"][0, :, 50, 0] = 0x7E                               # 448
+    t["ks"][0, :, 50] = 127
+    c.own.k64[0][:, 50] = 0.0
+    c.own.k64[0][:, 50, 0] = 448.0
+    c.q[..., 0] = 4.0                                        # its score: 158 nats
+    c.call()
+    torch.cuda.synchronize()
+    check_tight(c, floor=largest(c) * 2.0 ** -70)

@@ -324,7 +324,7 @@ bastion_status context_attn(const char *what, bool q8, const void *q, const void
       return fail(BASTION_ERR_CUDA, w + ": tree tensor map");
   }
   const bst::CtxGeo a{own.ks, own.vs, own.rows}, b{pre.ks, pre.vs, pre.rows};
-  cudaError_t e = bst::launch_ctx_attn(work, d, q8, maps, a, b, q, mask, scale, out, st);
+  cudaError_t e = bst::launch_ctx_attn(work, d, q8, maps, a, b, q, v_tree, mask, scale, out, st);
   if (e != cudaSuccess) return cuda_fail(e, what);
   return BASTION_OK;
 }

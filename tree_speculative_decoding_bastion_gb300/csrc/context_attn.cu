@@ -90,6 +90,7 @@ struct CtxParams {
   AttnWork w;
   CtxGeo own, prefix;
   const uint16_t *q;
+  const uint16_t *vt;                   // the tree's values (their size; the tiles come by TMA)
   const uint32_t *mask;                 // 32-bit words of the ancestor masks
   float scale_log2;
   uint16_t *out;
@@ -105,7 +106,7 @@ struct CtxBars {
   uint32_t tmem_base;
   int abort;
   int unset[CT_GROUPS];                 // a row of the group has seen no key yet
-  int scale[CT_GROUPS];                 // at the end of a piece: the exponent that the group's O is held at
+  int top_ctx, top_tree;                // 8-bit cache: largest V scale byte of the piece's keys, and the one that the tree's values would have
   AttnShare share;
 };
 
@@ -340,6 +341,69 @@ struct CtxSoftmax {
   static constexpr float TH = Q8 ? 7.f : 8.f;
   static constexpr float HEAD = Q8 ? 0.f : 16.f;
   static constexpr int SHIFT = 8;
+  static constexpr int LOWEST = -100;  // smallest exponent that V scales are held against
+
+  // The largest scale byte of the V rows of the piece's context that this thread
+  // looks at (byte 255 is a NaN, not a size).  Eight keys at a time where the scales lie
+  // in aligned words of eight: a read of 1/128 of the piece's bytes.  (A key at a time: 16
+  // single tokens over 512 to 8192 keys 61 us for 56.  What it costs beside taking the
+  // exponent from the first keys, which later ones may exceed by far: there 55, for
+  // 64 single tokens behind 8192 keys, with 512 short units, 45 -> 48.)
+  static BST_DEV int top_context(const CtxParams &p, const AttnPiece &pc, int tid) {
+    const CtxGeo &geo = pc.prefix ? p.prefix : p.own;
+    const int first = pc.t0 * CA_KEYS, stop = min(pc.L, min(pc.t1, pc.ctx_tiles) * CA_KEYS);
+    const bool paged = geo.rows.block_table != nullptr;
+    const bool words = ((reinterpret_cast<uintptr_t>(geo.vs) | (paged ? 0 : geo.rows.L_max)) & 7) == 0;
+    const int shift = paged ? 31 - __clz(geo.rows.page_size) : 0;
+    const int32_t *pages = paged ? geo.rows.block_table + static_cast<int64_t>(pc.b) * geo.rows.max_pages : nullptr;
+    const uint32_t base = static_cast<uint32_t>(paged ? pc.kvh : (static_cast<int64_t>(pc.b) * p.w.Hkv + pc.kvh) * geo.rows.L_max);
+    auto scale_at = [&](int key) -> const uint8_t * {          // NULL: a bad page
+      uint32_t row = base + static_cast<uint32_t>(key);
+      if (paged) {
+        const uint32_t page = static_cast<uint32_t>(__ldg(pages + (key >> shift)));
+        if (page >= static_cast<uint32_t>(geo.rows.num_pages)) return nullptr;
+        row = ((page * static_cast<uint32_t>(p.w.Hkv) + base) << shift) + (key & ((1 << shift) - 1));
+      }
+      return geo.vs + row;
+    };
+    if (words) {
+      uint32_t top4 = 0;
+#pragma unroll 4
+      for (int key = first + 8 * tid; key < stop; key += 8 * CT_SM) {
+        const uint8_t *at = scale_at(key);
+        if (!at) continue;
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(at));
+        const int n = stop - key;              // bytes that count
+        const uint32_t m0 = n >= 4 ? ~0u : ~(~0u << (8 * n)), m1 = n >= 8 ? ~0u : n <= 4 ? 0u : ~(~0u << (8 * (n - 4)));
+        const uint32_t a = w.x & m0 & ~__vcmpeq4(w.x, ~0u), c = w.y & m1 & ~__vcmpeq4(w.y, ~0u);
+        top4 = __vmaxu4(top4, __vmaxu4(a, c));
+      }
+      return static_cast<int>(max(max(top4 & 255u, (top4 >> 8) & 255u), max((top4 >> 16) & 255u, top4 >> 24)));
+    }
+    int top = 0;
+#pragma unroll 4
+    for (int key = first + tid; key < stop; key += CT_SM) {
+      const uint8_t *at = scale_at(key);
+      const int byte = at ? __ldg(at) : 0;
+      top = max(top, byte == 255 ? 0 : byte);
+    }
+    return top;
+  }
+  // ... and the one that the tree's values would have as one row.
+  static BST_DEV int top_tree(const CtxParams &p, const AttnPiece &pc, int tid) {
+    if (pc.t1 <= pc.ctx_tiles) return 0;
+    constexpr int CPR = D / 8;                 // 16-byte chunks of a row
+    uint32_t top = 0;
+#pragma unroll 2
+    for (int i = tid; i < pc.nb * CPR; i += CT_SM) {
+      const int64_t row = (static_cast<int64_t>(pc.b) * p.w.n_max + i / CPR) * p.w.Hkv + pc.kvh;
+      float x[8];
+      unpack16<BF16Tag>(__ldg(reinterpret_cast<const uint4 *>(p.vt + row * D) + i % CPR), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, finite_abs_bits(x[e]));
+    }
+    return static_cast<int>(q8_scale_byte(top));
+  }
 
   // The piece's rows of Q into shared memory: bf16 for bf16 tiles, two e4m3
   // parts and the row scale for 8-bit ones.
@@ -352,7 +416,8 @@ struct CtxSoftmax {
   // amax their last bits (4 trees of 128 over 32768 keys: 470 us for 520; a small tree's
   // one more barrier: 32.1 for 30.9).
   static constexpr int COMMON = 3;
-  static BST_DEV float load_q(const CtxParams &p, uint8_t *smem, int rows, bool need16, bool need8, int tid) {
+  static BST_DEV float load_q(const CtxParams &p, uint8_t *smem, CtxBars *bars, const AttnPiece &pc, int rows, int tid) {
+    const bool need16 = !Q8 || pc.t1 > pc.ctx_tiles, need8 = Q8 && pc.t0 < pc.ctx_tiles;
     constexpr int CPR = D / 8;                 // 16-byte chunks of a row
     constexpr int STEP = CT_SM / CPR;          // rows per pass
     const int *table = reinterpret_cast<const int *>(smem + LY::TAB_OFF);
@@ -366,6 +431,10 @@ struct CtxSoftmax {
         const int at = table[r];
         if (at >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(at) * D) + c);
       }
+    }
+    if constexpr (Q8) {                        // the sizes of V, while the rows are on their way
+      const int ctx = __reduce_max_sync(FULL, top_context(p, pc, tid)), tree = __reduce_max_sync(FULL, top_tree(p, pc, tid));
+      if ((tid & 31) == 0) atomicMax(&bars->top_ctx, ctx), atomicMax(&bars->top_tree, tree);
     }
     float common = 0.f;
     if constexpr (!Q8) {
@@ -560,7 +629,10 @@ struct CtxSoftmax {
     float2 l[HR / 2];
 #pragma unroll
     for (int i = 0; i < HR / 2; ++i) l[i] = make_float2(0.f, 0.f);
-    int E = 0;               // exponent that V scales are held against
+    // The exponent that V scales are held against: the largest of the piece, so that no
+    // key's lies above, and at least LOWEST (values below 2^-100 may come out as zero).
+    const int E = Q8 ? max(max(bars->top_ctx, bars->top_tree), LOWEST + 127) - 127 : 0;
+    const int ev_tree = Q8 ? max(bars->top_tree, LOWEST + 127) - 127 : 0;
     bool unset = true;       // uniform over the group: a row has seen no key
     float low = 0.f;         // bf16 tiles: the lowest of the rows' references
     const bool own = common == 0.f;          // 8-bit tiles: every row of Q has a scale of its own
@@ -589,15 +661,6 @@ struct CtxSoftmax {
       if (Q8 && ok_n) kb_n = __ldg(k_scales + row), vb_n = __ldg(v_scales + row);
       next_page(pos + STEP * CA_KEYS);
     };
-    if (Q8 && t_first < min(pc.t1, pc.ctx_tiles)) {
-      // the largest V scale of the first 32 keys (every warp reads the same): any
-      // exponent near the values' own will do, it only has to keep the sums in
-      // range; zero rows at the front must not drag it to -127
-      next_page(t_first * CA_KEYS + lane);
-      next_key(t_first * CA_KEYS + lane);
-      E = __reduce_max_sync(FULL, ok_n ? static_cast<int>(vb_n) - 127 : -60);
-      E = max(-60, min(60, E));
-    }
     next_page(t_first * CA_KEYS + key);
     next_key(t_first * CA_KEYS + key);
 
@@ -611,7 +674,7 @@ struct CtxSoftmax {
       if constexpr (TREE) {
         kx.valid = (t - pc.ctx_tiles) * CA_KEYS + key < pc.nb;
         kx.ck = 1.f;
-        kx.ev = 0;
+        kx.ev = ev_tree;
         // lane i: the mask word of row i over this warp's keys
         const int W32 = ((w.n_max + 63) >> 6) * 2;
         const int word = (t - pc.ctx_tiles) * 4 + kq;
@@ -633,7 +696,10 @@ struct CtxSoftmax {
       tc_fence_after();
       const float cs = F8 ? (own ? kx.ck : kx.ck * common) : p.scale_log2;
       const float2 cs2 = make_float2(cs, cs);
-      const float dev = Q8 ? static_cast<float>(kx.ev - E) : 0.f;   // the key's V scale, log2
+      // What the key adds to a score that is held against a reference (log2): its V
+      // scale, but no less than TH - 64, so that the row sum, which V scales do not
+      // enter, stays finite (a score is at most 2^64 above its reference).
+      const float lift = Q8 ? fmaxf(static_cast<float>(kx.ev - E), TH - 64.f) : 0.f;
       // ---- do the rows' references hold for this tile?
       bool raised = unset;
       if (!unset) {
@@ -668,8 +734,7 @@ struct CtxSoftmax {
             if constexpr (TREE) hide<C>(bits, c, kx.valid, x);
             most = fmaxf(most, largest(x));
           }
-          // (a key of a far smaller V scale must not overflow the sum either)
-          mine = kx.valid && (most + dev > TH || (Q8 && most > 64.f));
+          mine = kx.valid && most + lift > TH;
           over = vote_group(grp, mine);
         }
         raised = over;
@@ -685,8 +750,8 @@ struct CtxSoftmax {
             if (kx.valid) {
 #pragma unroll
               for (int i = 0; i < C; ++i) {
-                const float z = Q8 ? fmaxf(y[i] + dev, y[i] - 64.f) : y[i];
-                if (y[i] + dev > TH || (Q8 && y[i] > 64.f)) atomicMax(&xm[c + i], ordered(z));
+                const float z = y[i] + lift;
+                if (z > TH) atomicMax(&xm[c + i], ordered(z));
               }
             }
           }
@@ -696,7 +761,6 @@ struct CtxSoftmax {
         // this tile's keys, for all rows
         if (t != t_first) bar_group(grp);    // the last such tile's flag and maxima are read and reset
         float mx = -CUDART_INF_F;
-        const float lift = fmaxf(dev, -64.f);   // (as below: the sum must not overflow)
 #pragma unroll
         for (int c = 0; c < HR; c += C) {
           float x[C];
@@ -782,7 +846,8 @@ struct CtxSoftmax {
         mbar_wait(&bars->pv_done[(idx - 1) & 1], ((idx - 1) >> 1) & 1, abort, CT_WAIT_NS);
         __syncwarp();
       }
-      const float wj = !Q8 ? 1.f : kx.valid ? pow2i(kx.ev - E + SHIFT) : 0.f;   // 2^(dev + SHIFT)
+      // with its V scale (a tree's value carries its own), in units of 2^(E - SHIFT)
+      const float wj = !Q8 ? 1.f : !kx.valid ? 0.f : pow2i((TREE ? 0 : kx.ev) - E + SHIFT);
       const float2 w2 = make_float2(wj, wj);
 #pragma unroll
       for (int c = 0; c < HR; c += C) {
@@ -885,7 +950,6 @@ struct CtxSoftmax {
       const float sum = across_lanes<HR>(v);
       if (lane < HR) part[kq * CT_R + lane] = sum;
     }
-    if (key == 0) bars->scale[grp] = E;
     if (TWO)
       bar_softmax();
     else
@@ -894,8 +958,8 @@ struct CtxSoftmax {
     float *slot = w.slots + piece_slot(w, cta, pc.t0 == 0, pc.unit) * slot_floats(CT_R, D);
     if (key < HR && stream == 0) {
       auto state_sum = [&](int i) { return (part[i] + part[CT_R + i]) + (part[2 * CT_R + i] + part[3 * CT_R + i]); };
-      auto unit = [&](int g) { return Q8 ? pow2i(*const_cast<volatile int *>(&bars->scale[g]) - SHIFT) : 1.f; };
-      float sum = state_sum(key), m = mref[key], f0 = unit(grp), f1 = 0.f;
+      const float unit = Q8 ? pow2i(E - SHIFT) : 1.f;
+      float sum = state_sum(key), m = mref[key], f0 = unit, f1 = 0.f;
       if (TWO) {
         // the two streams' sums and outputs, against the larger reference
         const float m1 = mref[64 + key], top = fmaxf(m, m1);
@@ -903,7 +967,7 @@ struct CtxSoftmax {
         sum = sum * a + state_sum(64 + key) * b;
         m = top;
         f0 *= a;
-        f1 = b * unit(grp + 2);
+        f1 = b * unit;
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;        // a row that sees no key is zero
       rise[key] = f0 * inv;
@@ -1262,10 +1326,11 @@ __global__ void __launch_bounds__(CT_THREADS, 1) ctx_attn_kernel(const __grid_co
         bar_softmax();
       }
       row_table(w, pc, starts, tid, CT_SM, table);
+      if (Q8 && tid == 0) bars->top_ctx = bars->top_tree = 0;
       if (tid < CT_R)
         mref[tid] = CT_UNSET, reinterpret_cast<int *>(smem + LY::XM_OFF)[tid] = ORDERED_LOWEST;
       bar_softmax();
-      const float common = SM::load_q(p, smem, N, !Q8 || pc.t1 > pc.ctx_tiles, Q8 && pc.t0 < pc.ctx_tiles, tid);
+      const float common = SM::load_q(p, smem, bars, pc, N, tid);
       warp_arrive(&bars->q_full, 1);
       if (Q8) bar_softmax();                 // the row scales, and `xm` as the tiles want it
       if (RM == 128 && N == 128) {
@@ -1314,13 +1379,14 @@ cudaError_t prepare_ctx_attn() {
 }
 
 cudaError_t launch_ctx_attn(const AttnWork &w, int d, bool q8, const CtxMaps &maps, const CtxGeo &own,
-                            const CtxGeo &prefix, const void *q, const uint64_t *mask, float scale, void *out,
-                            cudaStream_t stream) {
+                            const CtxGeo &prefix, const void *q, const void *vt, const uint64_t *mask, float scale,
+                            void *out, cudaStream_t stream) {
   CtxParams p{};
   p.w = w;
   p.own = own;
   p.prefix = prefix;
   p.q = static_cast<const uint16_t *>(q);
+  p.vt = static_cast<const uint16_t *>(vt);
   p.mask = reinterpret_cast<const uint32_t *>(mask);
   p.scale_log2 = scale * kLog2e;
   p.out = static_cast<uint16_t *>(out);

@@ -31,8 +31,8 @@ struct CtxMaps {
 cudaError_t prepare_ctx_attn();
 cudaError_t prepare_ctx_attn_f32();
 cudaError_t launch_ctx_attn(const AttnWork &w, int d, bool q8, const CtxMaps &maps, const CtxGeo &own,
-                            const CtxGeo &prefix, const void *q, const uint64_t *mask, float scale, void *out,
-                            cudaStream_t stream);
+                            const CtxGeo &prefix, const void *q, const void *vt, const uint64_t *mask, float scale,
+                            void *out, cudaStream_t stream);
 cudaError_t launch_ctx_attn_f32(const AttnWork &w, int d, bool q8, const RowSource &own, const RowSource &prefix,
                                 const float *q, const float *kt, const float *vt, const uint64_t *mask, float scale,
                                 float *out, cudaStream_t stream);
