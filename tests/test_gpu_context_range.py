@@ -244,3 +244,28 @@ def test_a_dominating_key_of_a_tiny_value(ctx):
     c.call()
     torch.cuda.synchronize()
     check_tight(c, floor=largest(c) * 2.0 ** -70)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("which", ["vs", "ks"])
+@pytest.mark.parametrize("rows", [1, 12, 40])
+@pytest.mark.parametrize("weight", [1.0, 0.0])
+def test_a_scale_byte_of_255_is_nan(weight, rows, which, dtype):
+    """A context key whose K or V scale is the format's NaN makes the rows of its KV head
+    NaN, whatever its codes and its weight; the other heads stay as they were."""
+    c = Case(68, [rows, 1], rows, 8, 2, 128, dtype, True, 16, [700, 40], 300, 16)
+    c.call()
+    torch.cuda.synchronize()
+    clean = c.out.clone()
+    at, slot = int(c.own.table[0, 600 // 16]), 600 % 16
+    c.own.t[which][at, 1, slot] = 255
+    c.own.t["v"][at, 1, slot] = 0
+    if weight == 0.0:                                         # a score some 10^5 below the others'
+        c.own.t["k"][at, 1, slot] = torch.where(c.q[0, 0, 4].float() > 0, 0xFE, 0x7E).to(torch.uint8)
+        if which == "vs":
+            c.own.t["ks"][at, 1, slot] = 127 + 8
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    assert torch.isnan(c.out[0, :rows, 4:]).all()
+    assert torch.equal(c.out[0, :rows, :4], clean[0, :rows, :4]) and torch.equal(c.out[1, :1], clean[1, :1])

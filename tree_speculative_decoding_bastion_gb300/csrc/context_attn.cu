@@ -316,7 +316,7 @@ BST_DEV float pow2i(int k) { return k < -126 ? 0.f : __int_as_float((min(k, 127)
 struct CtxKey {
   bool valid;
   float ck;     // 2^(exponent of the K scale)
-  int ev;       // exponent of the V scale
+  int ev;       // exponent of the V scale; 128: the format's NaN
 };
 
 // Position of the softmax warps in the CTA's whole range: S^T / P tiles and
@@ -847,7 +847,8 @@ struct CtxSoftmax {
         __syncwarp();
       }
       // with its V scale (a tree's value carries its own), in units of 2^(E - SHIFT)
-      const float wj = !Q8 ? 1.f : !kx.valid ? 0.f : pow2i((TREE ? 0 : kx.ev) - E + SHIFT);
+      // (a NaN makes every row NaN that sees the key: all of them)
+      const float wj = !Q8 ? 1.f : !kx.valid ? 0.f : kx.ev == 128 ? CUDART_NAN_F : pow2i((TREE ? 0 : kx.ev) - E + SHIFT);
       const float2 w2 = make_float2(wj, wj);
 #pragma unroll
       for (int c = 0; c < HR; c += C) {
