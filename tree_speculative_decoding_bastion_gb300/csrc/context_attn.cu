@@ -316,7 +316,7 @@ BST_DEV float pow2i(int k) { return k < -126 ? 0.f : __int_as_float((min(k, 127)
 struct CtxKey {
   bool valid;
   float ck;     // 2^(exponent of the K scale)
-  int ev;       // exponent of the V scale; 128: the format's NaN
+  int ev;       // exponent of the V scale
 };
 
 // Position of the softmax warps in the CTA's whole range: S^T / P tiles and
@@ -682,7 +682,9 @@ struct CtxSoftmax {
         if (at >= 0 && word < W32) bits = __ldg(p.mask + static_cast<int64_t>(at / w.Hq) * W32 + word);
       } else {
         kx.valid = ok_n;
-        kx.ck = F8 ? q8_scale(kb_n) : 1.f;
+        // (a V scale that is the format's NaN, too, makes the key's scores NaN: it
+        // turns every row that sees it into NaN)
+        kx.ck = F8 ? q8_scale(vb_n == 255u ? 255u : kb_n) : 1.f;
         kx.ev = F8 ? static_cast<int>(vb_n) - 127 : 0;
         next_key((t + STEP) * CA_KEYS + key);
       }
@@ -847,8 +849,7 @@ struct CtxSoftmax {
         __syncwarp();
       }
       // with its V scale (a tree's value carries its own), in units of 2^(E - SHIFT)
-      // (a NaN makes every row NaN that sees the key: all of them)
-      const float wj = !Q8 ? 1.f : !kx.valid ? 0.f : kx.ev == 128 ? CUDART_NAN_F : pow2i((TREE ? 0 : kx.ev) - E + SHIFT);
+      const float wj = !Q8 ? 1.f : !kx.valid ? 0.f : pow2i((TREE ? 0 : kx.ev) - E + SHIFT);
       const float2 w2 = make_float2(wj, wj);
 #pragma unroll
       for (int c = 0; c < HR; c += C) {
