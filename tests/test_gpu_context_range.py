@@ -269,3 +269,20 @@ def test_a_scale_byte_of_255_is_nan(weight, rows, which, dtype):
     assert int(c.err) == 0
     assert torch.isnan(c.out[0, :rows, 4:]).all()
     assert torch.equal(c.out[0, :rows, :4], clean[0, :rows, :4]) and torch.equal(c.out[1, :1], clean[1, :1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,g", [(4, 4), (8, 4), (16, 4), (32, 4), (50, 4)])
+@pytest.mark.parametrize("ctx", [37, 1500])
+@pytest.mark.parametrize("lo,hi", [(-5, 3), (-20, 3), (-2, 0)])
+def test_rows_of_q_of_different_sizes(lo, hi, ctx, N, g, d):
+    """Sizes of 2^lo to 2^hi among the rows of one tile, and a row of zeros: rows whose 8-bit
+    parts have scales of their own (and, for the last range, a common one)."""
+    c = Case(69, [N, max(1, N - 3)], N, 2 * g, 2, d, "bf16", True, 16, [ctx, 20], None)
+    r = torch.Generator().manual_seed(69)
+    size = torch.exp2(torch.randint(lo, hi + 1, (2, N, 2 * g, 1), generator=r).float()).cuda()
+    c.q.copy_((c.q.float() * size).to(torch.bfloat16))
+    c.q[0, N // 2, 1] = 0.0
+    c.call()
+    torch.cuda.synchronize()
+    check_tight(c)
