@@ -54,7 +54,8 @@ cudaError_t launch_kv_commit(const void *k_tree, const void *v_tree, int esz, in
 cudaError_t launch_kv_write_q8(const void *k_new, const void *v_new, bool bf16, int B, int T, int Hkv, int d, int K,
                                const int32_t *count, const int32_t *nodes, void *k, void *v, uint8_t *ks, uint8_t *vs,
                                int64_t L_max, const int32_t *block_table, int max_pages, int num_pages, int page_size,
-                               const int32_t *ctx_len, int32_t *ctx_out, uint32_t *dev_err, cudaStream_t stream);
+                               const int32_t *ctx_len, int32_t *ctx_out, uint32_t *dev_err, int sms,
+                               cudaStream_t stream);
 cudaError_t launch_kv_read_q8(const void *k, const void *v, const uint8_t *ks, const uint8_t *vs, int64_t L_max,
                               const int32_t *block_table, int max_pages, int num_pages, int page_size, bool bf16,
                               int B, int T, int Hkv, int d, const int32_t *start, const int32_t *count, void *k_out,
@@ -639,7 +640,7 @@ bastion_status bastion_kv_append_q8(const void *k_new, const void *v_new, bastio
   if (s != BASTION_OK) return s;
   cudaError_t e = bst::launch_kv_write_q8(k_new, v_new, dtype == BASTION_BF16, B, T, Hkv, d, 0, n_new, nullptr, kv->k,
                                           kv->v, kv->k_scale, kv->v_scale, kv->L_max, kv->block_table, kv->max_pages,
-                                          kv->num_pages, kv->page_size, ctx_len, ctx_out, dev_err,
+                                          kv->num_pages, kv->page_size, ctx_len, ctx_out, dev_err, sms,
                                           reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_append_q8 launch");
   return BASTION_OK;
@@ -661,7 +662,7 @@ bastion_status bastion_kv_commit_q8(const void *k_tree, const void *v_tree, bast
   cudaError_t e = bst::launch_kv_write_q8(k_tree, v_tree, dtype == BASTION_BF16, B, n_max, Hkv, d, K, acc_len,
                                           acc_nodes, kv->k, kv->v, kv->k_scale, kv->v_scale, kv->L_max,
                                           kv->block_table, kv->max_pages, kv->num_pages, kv->page_size, ctx_len,
-                                          ctx_out, dev_err, reinterpret_cast<cudaStream_t>(stream));
+                                          ctx_out, dev_err, sms, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_commit_q8 launch");
   return BASTION_OK;
 }

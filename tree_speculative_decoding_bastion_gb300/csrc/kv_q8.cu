@@ -15,6 +15,8 @@
 // (8 heads of 128, 228 MB) 50 us, 4.6 TB/s; 16 contexts of up to 8192 read back
 // to bf16 (536 MB) 85.6 us, 6.3 TB/s; one token 3.5 us, 16 accepted paths 6.6 us
 // (dependent loads: counts, page or node, row).
+#include <algorithm>
+
 #include "q8.cuh"
 
 namespace bst {
@@ -74,7 +76,8 @@ struct WriteParams {
   uint4 *k, *v;                  // codes
   uint8_t *ks, *vs;              // scale bytes
   RowCache cache;
-  int T, Hkv, d, K;              // K: commit, columns of nodes - 1
+  int T, Hkv, K;                 // K: commit, columns of nodes - 1
+  int passes;                    // how often a CTA of the grid goes on to the next rows (kv_q8_write_kernel)
   int lanes, gs;                 // d / 16 lanes hold a row; gs: the power of two at or above
   const int32_t *count;          // append: tokens per request; commit: acc_len (tokens - 1)
   const int32_t *nodes;          // commit: [B, K + 1] rows of k_new; append: NULL (row i)
@@ -110,10 +113,26 @@ BST_DEV uint32_t write_checks(const WriteParams &p, int b, const WriteRequest &r
       if (node < 0 || node >= p.T) bad |= BASTION_DEVERR_N;
     }
   if (p.cache.block_table && r.cnt > 0) {
+    // page ids first .. end - 1, four at a time where they lie in aligned words of four
     const int32_t *row = p.cache.block_table + static_cast<int64_t>(b) * p.cache.max_pages;
-    const int last = (r.ctx + r.cnt - 1) / p.cache.page_size;
-    for (int i = r.ctx / p.cache.page_size + threadIdx.x; i <= last; i += threads)
-      if (row[i] < 0 || row[i] >= p.cache.num_pages) bad |= BASTION_DEVERR_PAGE;
+    const int first = r.ctx / p.cache.page_size, end = (r.ctx + r.cnt - 1) / p.cache.page_size + 1;
+    const int head = min(end, first + static_cast<int>((0 - (reinterpret_cast<uintptr_t>(row + first) >> 2)) & 3));
+    const int fours = (end - head) >> 2;
+    const int4 *four = reinterpret_cast<const int4 *>(row + head);
+    const uint32_t pages = static_cast<uint32_t>(p.cache.num_pages);
+    uint32_t top = 0;                         // (a negative id is a large one)
+#pragma unroll 4
+    for (int i = threadIdx.x; i < fours; i += threads) {
+      const int4 v = __ldg(four + i);
+      top = max(max(top, max(static_cast<uint32_t>(v.x), static_cast<uint32_t>(v.y))),
+                max(static_cast<uint32_t>(v.z), static_cast<uint32_t>(v.w)));
+    }
+    const int rest = (head - first) + (end - head - 4 * fours);   // at most six, before and behind
+    if (static_cast<int>(threadIdx.x) < rest) {
+      const int i = first + static_cast<int>(threadIdx.x);
+      top = max(top, static_cast<uint32_t>(__ldg(row + (i < head ? i : i + 4 * fours))));
+    }
+    if (top >= pages) bad |= BASTION_DEVERR_PAGE;
   }
   return bad;
 }
@@ -168,7 +187,9 @@ struct WriteRows {
 // Many tokens: CTA (x, b) takes a stretch of consecutive rows of request b;
 // kv_q8_advance_kernel then moves ctx_out.  128 bytes a lane in flight and four
 // CTAs an SM: with five and six 51.7 and 57.7 us for 48.7, with half, one and a
-// half and twice the rows a lane 50.8, 52.8 and 55.
+// half and twice the rows a lane 50.8, 52.8 and 55.  Every CTA checks all pages of
+// its request before it writes, so its stretch grows with the request's pages
+// (launch_kv_write_q8): the checks read a part of what the rows read, not its square.
 template <class Tag>
 __global__ void __launch_bounds__(Q8_THREADS, 4) kv_q8_write_kernel(const WriteParams p) {
   constexpr int U = q8_write_unroll<Tag>();
@@ -176,23 +197,29 @@ __global__ void __launch_bounds__(Q8_THREADS, 4) kv_q8_write_kernel(const WriteP
   pdl_wait();
   pdl_trigger();
   const int per_pass = Q8_THREADS / p.gs;
-  const int r0 = blockIdx.x * per_pass * U;
+  const int r0 = blockIdx.x * p.passes * per_pass * U;
   const WriteRequest q = write_request(p, b);
   if (q.bad || r0 >= 2 * q.cnt * p.Hkv) return;     // uniform
-  const int r = r0 + static_cast<int>(threadIdx.x) / p.gs;
   const int lane_in_row = threadIdx.x & (p.gs - 1);
+  int r = r0 + static_cast<int>(threadIdx.x) / p.gs;
   WriteRows<Tag, U> rows;
   rows.load(p, b, q, r, per_pass, lane_in_row);
   if (__syncthreads_or(write_checks(p, b, q, Q8_THREADS) != 0)) return;
   rows.store(p, q, r, per_pass, lane_in_row);
+  const int end = min(r0 + p.passes * per_pass * U, 2 * q.cnt * p.Hkv);
+  for (int first = r0 + per_pass * U; first < end; first += per_pass * U) {   // uniform
+    r += per_pass * U;
+    rows.load(p, b, q, r, per_pass, lane_in_row);
+    rows.store(p, q, r, per_pass, lane_in_row);
+  }
 }
 
-__global__ void __launch_bounds__(Q8_THREADS) kv_q8_advance_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(Q8_ONE_THREADS) kv_q8_advance_kernel(const WriteParams p) {
   const int b = blockIdx.x;
   pdl_wait();   // the rows are written: nobody reads ctx_len any more, which ctx_out may be
   pdl_trigger();
   const WriteRequest q = write_request(p, b);
-  const uint32_t bad = q.bad ? q.bad : write_checks(p, b, q, Q8_THREADS);
+  const uint32_t bad = q.bad ? q.bad : write_checks(p, b, q, blockDim.x);
   if (bad) set_err(p.dev_err, bad);
   const bool ok = !__syncthreads_or(bad != 0);
   if (threadIdx.x == 0) p.ctx_out[b] = ok ? q.ctx + q.cnt : q.ctx;
@@ -318,7 +345,8 @@ static int group_of(int lanes) {
 cudaError_t launch_kv_write_q8(const void *k_new, const void *v_new, bool bf16, int B, int T, int Hkv, int d, int K,
                                const int32_t *count, const int32_t *nodes, void *k, void *v, uint8_t *ks, uint8_t *vs,
                                int64_t L_max, const int32_t *block_table, int max_pages, int num_pages, int page_size,
-                               const int32_t *ctx_len, int32_t *ctx_out, uint32_t *dev_err, cudaStream_t stream) {
+                               const int32_t *ctx_len, int32_t *ctx_out, uint32_t *dev_err, int sms,
+                               cudaStream_t stream) {
   WriteParams p{};
   p.k_new = static_cast<const uint4 *>(k_new);
   p.v_new = static_cast<const uint4 *>(v_new);
@@ -329,7 +357,6 @@ cudaError_t launch_kv_write_q8(const void *k_new, const void *v_new, bool bf16, 
   p.cache = RowCache{L_max, block_table, max_pages, num_pages, page_size};
   p.T = T;
   p.Hkv = Hkv;
-  p.d = d;
   p.K = K;
   p.lanes = d / 16;
   p.gs = group_of(p.lanes);
@@ -354,13 +381,24 @@ cudaError_t launch_kv_write_q8(const void *k_new, const void *v_new, bool bf16, 
     return bf16 ? cudaLaunchKernelEx(&cfg, kv_q8_write_one_kernel<BF16Tag>, p)
                 : cudaLaunchKernelEx(&cfg, kv_q8_write_one_kernel<F32Tag>, p);
   }
-  const int per_cta = Q8_THREADS / p.gs * (bf16 ? q8_write_unroll<BF16Tag>() : q8_write_unroll<F32Tag>());
-  cfg.gridDim = dim3(static_cast<unsigned>((2 * most + per_cta - 1) / per_cta), B, 1);
+  const int per_pass = Q8_THREADS / p.gs * (bf16 ? q8_write_unroll<BF16Tag>() : q8_write_unroll<F32Tag>());
+  const int64_t all = (2 * most + per_pass - 1) / per_pass;
+  // Stretches so long that the page ids a CTA reads are at most 1/16 of the bytes that it
+  // moves, as far as the grid still fills the GPU (131072 tokens of 8 heads of 128 in
+  // bf16: pages of 8 192 us, of 64 182, of one token 260; one pass a CTA and page ids
+  // one by one 294, 197 and 1165; without pages 154).
+  const int64_t page_bytes = block_table ? 4 * (static_cast<int64_t>(T) / page_size + 1) : 0;
+  const int64_t pass_bytes = static_cast<int64_t>(per_pass) * (d * (bf16 ? 2 : 4) + d + 1);
+  const int64_t fill = std::max<int64_t>(1, all * B / (4 * sms));
+  p.passes = static_cast<int>(std::min(fill, (16 * page_bytes + pass_bytes - 1) / pass_bytes));
+  p.passes = std::max(p.passes, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((all + p.passes - 1) / p.passes), B, 1);
   cfg.blockDim = dim3(Q8_THREADS, 1, 1);
   cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, kv_q8_write_kernel<BF16Tag>, p)
                        : cudaLaunchKernelEx(&cfg, kv_q8_write_kernel<F32Tag>, p);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(B, 1, 1);
+  cfg.blockDim = dim3(page_bytes > 4096 ? Q8_ONE_THREADS : Q8_THREADS, 1, 1);   // a thread for every four page ids or so
   return cudaLaunchKernelEx(&cfg, kv_q8_advance_kernel, p);
 }
 
