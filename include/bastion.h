@@ -376,7 +376,8 @@ bastion_status bastion_kv_commit(const void *k_tree, const void *v_tree, bastion
  * e4m3 values nearest to x * 2^-e (round to nearest even; infinities saturate to
  * +-448, NaN stays NaN); the row stands for code * 2^e.  The scale byte is
  * e + 127 (e8m0).  Relative rounding error of an element: at most 2^-4, for
- * elements of at least 2^-14 of the row's amax.
+ * elements of at least 2^-13 of the row's amax (the scaled amax may lie just above
+ * 224, and e4m3's steps no longer shrink below 2^-6, 2^-13.8 of it).
  */
 typedef struct {
   void *k;                    /* e4m3 codes; contiguous: [B, Hkv, L_max, d]; paged: [num_pages, Hkv, page_size, d] */

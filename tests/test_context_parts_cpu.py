@@ -1,8 +1,16 @@
-"""The arithmetic of the 8-bit parts that the attention over the 8-bit cache makes
-of its softmax weights, over every value they can have."""
+"""The arithmetic of the 8-bit cache's rows, and of the 8-bit parts that the attention over
+it makes of its softmax weights, over every value they can have."""
+import os
+import re
+
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
+
+from oracle import context_oracle as co  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def cut(x):
@@ -31,3 +39,20 @@ def test_three_e5m2_parts_hold_a_weight():
     normal = x >= 2.0 ** -5
     rel = err[normal] / x[normal]
     assert float(rel.square().mean().sqrt()) <= 2.0 ** -11 and abs(float(rel.mean())) <= 2.0 ** -20
+
+
+def stated_range():
+    """The k of the header's "elements of at least 2^-k of the row's amax"."""
+    text = " ".join(open(os.path.join(ROOT, "include", "bastion.h")).read().replace("*", " ").split())
+    return int(re.search(r"at most 2\^-4, for elements of at least 2\^-(\d+) of the row's amax", text).group(1))
+
+
+@pytest.mark.parametrize("amax", [224.0 * (1 + 2.0 ** -20), 225.0, 300.0, 447.0, 448.0])
+def test_the_stated_relative_error_of_a_row(amax):
+    """Every element from the stated share of the amax on is within 2^-4 of itself, at the amax
+    that wastes most of the scale as well."""
+    low = amax * 2.0 ** -stated_range()
+    x = np.concatenate([[amax], np.geomspace(low, amax, 20001), [low]])[None]
+    codes, byte = co.q8_quantise(x)
+    assert int(byte[0]) == 127
+    assert np.all(np.abs(co.q8_value(codes, byte) - x) <= x * 2.0 ** -4)
