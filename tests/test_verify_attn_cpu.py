@@ -1,0 +1,30 @@
+"""What the verification attention's dispatch and the step refuse, without a GPU."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tree_speculative_decoding_bastion_gb300 import binding as bn  # noqa: E402
+
+
+class Calls:
+    """Stands in for the library: no call may reach it."""
+
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was called")
+
+
+def caches():
+    x = torch.zeros(1, 1, 8, 64)
+    return {"kv": bn.KV(x, x), "kvq8": bn.KVQ8.empty(1, 1, 8, 64, device="cpu")}
+
+
+@pytest.mark.parametrize("kind", ["kv", "kvq8"])
+@pytest.mark.parametrize("given", ["prefix", "prefix_len"])
+def test_a_prefix_and_its_length_come_together(monkeypatch, kind, given):
+    """A length without its prefix would be ignored, a prefix without a length has none."""
+    monkeypatch.setattr(bn, "_lib", Calls())
+    kv = caches()[kind]
+    x = torch.zeros(1, 1, 1, 64)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(bn.BastionError, match="come together"):
+        bn.verify_attn(x, x, x, kv, i, i, i, x, 1.0, **{given: kv if given == "prefix" else i})

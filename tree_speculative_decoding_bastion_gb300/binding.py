@@ -470,6 +470,8 @@ def verify_attn(q, k_tree, v_tree, kv, ctx_len, mask, n, out, scale: float, pref
     """Stage 3 by the kind of the caches: bastion_tree_attn_q8 for a KVQ8,
     bastion_tree_attn_shared for a KV behind a shared prefix, else
     bastion_tree_attn."""
+    if (prefix is None) != (prefix_len is None):
+        raise BastionError("prefix and prefix_len come together")
     kw = dict(ws=ws, dev_err=dev_err, stream=stream)
     if isinstance(kv, KVQ8):
         bastion_tree_attn_q8(q, k_tree, v_tree, kv, ctx_len, mask, n, out, scale, prefix=prefix, prefix_len=prefix_len, **kw)
