@@ -50,8 +50,8 @@
  * - The accept and tree_attn workspaces must be zero-filled once when
  *   allocated; every call leaves them as it needs them, so they can be reused
  *   without clearing (those of tree_attn_q8 and tree_attn_shared need no
- *   filling).  Two calls in flight at the same time must not share a
- *   workspace.
+ *   filling; what they leave in one must be zeroed before tree_attn takes it).
+ *   Two calls in flight at the same time must not share a workspace.
  */
 #ifndef BASTION_H
 #define BASTION_H

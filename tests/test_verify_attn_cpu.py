@@ -28,3 +28,26 @@ def test_a_prefix_and_its_length_come_together(monkeypatch, kind, given):
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(bn.BastionError, match="come together"):
         bn.verify_attn(x, x, x, kv, i, i, i, x, 1.0, **{given: kv if given == "prefix" else i})
+
+
+@pytest.mark.parametrize("made,given", [("kv", "kvq8"), ("kvq8", "kv")])
+def test_a_step_keeps_to_its_kind_of_cache(monkeypatch, made, given):
+    """The 8-bit attention leaves anything in the step's attention workspace, and the other
+    kind's wants it as its own calls leave it."""
+    class Tensors:
+        @staticmethod
+        def bastion_tree_attn_workspace_size(*args):
+            return 16
+
+        bastion_tree_attn_q8_workspace_size = bastion_accept_workspace_size = bastion_tree_attn_workspace_size
+
+    c = caches()
+    monkeypatch.setattr(bn, "_lib", Tensors())
+    step = bn.SpecTreeStep(1, 2, 16, 2, 1, 4, 1, 1, 64, c[made], device="cpu")
+    monkeypatch.setattr(bn, "_lib", Calls())
+    x = torch.zeros(1, 4, 1, 64)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(bn.BastionError, match="caches was given"):
+        step.verify(x, x, x, c[given], i, 1.0, x)
+    with pytest.raises(bn.BastionError, match="must be a CUDA tensor"):   # the right kind goes on to the call's checks
+        step.verify(x, x, x, c[made], i, 1.0, x)

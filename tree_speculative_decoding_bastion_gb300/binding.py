@@ -695,7 +695,8 @@ class SpecTreeStep:
     """Owns the output buffers and workspaces of one spec-tree step and runs the
     four library calls in order on the current stream (no host sync inside).
 
-    kv is a KV or an 8-bit KVQ8 cache.  prefix (a cache of one request, of kv's
+    kv is a KV or an 8-bit KVQ8 cache; the steps take caches of the same kind (the
+    attention workspace is that kind's).  prefix (a cache of one request, of kv's
     type) and prefix_len (int32 [1], device) are a context that every request
     begins with: kv and ctx_len then hold what follows it, and tree positions
     count from total_len (prefix and own context, int32 [B]) where the calls
@@ -706,6 +707,7 @@ class SpecTreeStep:
         if (prefix is None) != (prefix_len is None):
             raise BastionError("prefix and prefix_len come together")
         self.prefix, self.prefix_len = prefix, prefix_len
+        self.q8 = isinstance(kv, KVQ8)
         self.B, self.K, self.V, self.topk = B, K, V, topk
         self.n_min, self.n_max, self.Hq, self.Hkv, self.d = n_min, n_max, Hq, Hkv, d
         dev = torch.device(device)
@@ -748,7 +750,12 @@ class SpecTreeStep:
                            self.n, self.parent, self.token, self.depth, self.pos, self.rho, self.mask, self.ahat,
                            self.S, self.S_curve, dev_err=self.dev_err, stream=stream)
 
+    def _check_kind(self, kv) -> None:
+        if isinstance(kv, KVQ8) != self.q8:
+            raise BastionError(f"a step for {'KVQ8' if self.q8 else 'KV'} caches was given a {type(kv).__name__}")
+
     def verify(self, q, k_tree, v_tree, kv, ctx_len, scale, target, stream=None):
+        self._check_kind(kv)
         verify_attn(q, k_tree, v_tree, kv, ctx_len, self.mask, self.n, self.attn_out, scale, prefix=self.prefix,
                     prefix_len=self.prefix_len, ws=self.attn_ws, dev_err=self.dev_err, stream=stream)
         bastion_accept(target, self.n, self.parent, self.token, self.K, self.acc_len, self.acc_nodes, self.acc_tok,
@@ -758,6 +765,7 @@ class SpecTreeStep:
                  total_len=None):
         if self.prefix is not None and total_len is None:
             raise BastionError("a step behind a shared prefix takes total_len (prefix and own context)")
+        self._check_kind(kv)
         self.draft(logits, root_tok, ctx_len if total_len is None else total_len, C, L_AR, stream=stream)
         self.verify(q, k_tree, v_tree, kv, ctx_len, scale, target, stream=stream)
 
