@@ -51,3 +51,13 @@ def test_a_step_keeps_to_its_kind_of_cache(monkeypatch, made, given):
         step.verify(x, x, x, c[given], i, 1.0, x)
     with pytest.raises(bn.BastionError, match="must be a CUDA tensor"):   # the right kind goes on to the call's checks
         step.verify(x, x, x, c[made], i, 1.0, x)
+
+
+def test_workspace_sizes_want_one_kind_of_cache(monkeypatch):
+    monkeypatch.setattr(bn, "_lib", Calls())
+    c = caches()
+    for kv, prefix in ((c["kv"], c["kvq8"]), (c["kvq8"], c["kv"])):
+        with pytest.raises(bn.BastionError, match="takes KV"):
+            bn.verify_workspace_size(1, 4, 1, 1, 64, kv, prefix)
+    with pytest.raises(bn.BastionError, match="takes KVQ8"):
+        bn.bastion_tree_attn_q8_workspace_size(1, 4, 1, 1, 64, c["kv"])

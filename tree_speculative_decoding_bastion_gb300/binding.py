@@ -377,6 +377,9 @@ _CODES = {torch.float32: BASTION_F32, torch.bfloat16: BASTION_BF16}
 def _context_ws(name: str, B, n_max, Hq, Hkv, d, kv, prefix, dtype) -> int:
     if dtype not in _CODES:
         raise BastionError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    kind = KVQ8 if name.startswith("bastion_tree_attn_q8") else KV
+    if not isinstance(kv, kind) or not (prefix is None or isinstance(prefix, kind)):
+        raise BastionError(f"{name} takes {kind.__name__} caches")
     p = None if prefix is None else ctypes.pointer(prefix.c_struct())
     return int(getattr(lib(), name)(_CODES[dtype], B, n_max, Hq, Hkv, d, ctypes.pointer(kv.c_struct()), p))
 
