@@ -64,8 +64,8 @@
 // keys 230 us), an 8-bit tile of few rows 1.9 thousand, bound by latency (16 tokens
 // over 512 to 8192 keys 44 us, 3.6 TB/s).
 // Every mbarrier wait is bounded in time; after an expiry the CTA issues no
-// further copies, walks its loops to the end without waiting and reports
-// BASTION_DEVERR_TIMEOUT.
+// further copies, walks its loops to the end with at most two polls a wait and
+// reports BASTION_DEVERR_TIMEOUT.
 #include <type_traits>
 
 #include "context_attn.cuh"

@@ -51,12 +51,10 @@ BST_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0u) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > limit_ns) {
-        *abort = 1;
-        return false;
-      }
+    if (*abort) return false;                // (before the first poll it would cost 2 to 3% of the attention)
+    if ((it & 63u) == 0u && globaltimer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
     }
   }
 }
