@@ -59,10 +59,10 @@
 // 2 m - 1.
 // Measured: a CTA begins its first tile 5 us after launch (the partition 2, Q, the
 // first references); then an 8-bit tile of 128 rows takes 4.9 thousand cycles, bound by the
-// softmax's instructions (4 trees of 128 over 32768 keys
-// 520 us), a bf16 one 2.4 thousand (16 trees behind 16381 shared
-// keys 230 us), an 8-bit tile of few rows 1.9 thousand, bound by latency (16 tokens
-// over 512 to 8192 keys 44 us, 3.6 TB/s).
+// softmax's instructions (issue slots 50% busy, tensor pipe 29%: 4 trees of 128
+// over 32768 keys 531 us), a bf16 one 2.4 thousand (16 trees behind 16381 shared
+// keys 232 us), an 8-bit tile of few rows 1.9 thousand, bound by latency (16 tokens
+// over 512 to 8192 keys 45.5 us, 3.5 TB/s).
 // Every mbarrier wait is bounded in time; after an expiry the CTA issues no
 // further copies, walks its loops to the end with at most two polls a wait and
 // reports BASTION_DEVERR_TIMEOUT.
@@ -412,9 +412,11 @@ struct CtxSoftmax {
   // as many MMAs, whose count and not whose size costs there.
   // Returns the rows' common scale (times scale log2(e)) where there is one, else
   // 0: rows whose own scales lie within 2^COMMON take the largest, which saves two
-  // multiplications a score and costs elements below 2^-6.8 (not 2^-9.8) of a row's
-  // amax their last bits (4 trees of 128 over 32768 keys: 470 us for 520; a small tree's
-  // one more barrier: 32.1 for 30.9).
+  // multiplications a score (4 trees of 128 over 32768 keys: 527 us for 566, 16 trees of
+  // 8 to 64 204 for 214) and costs elements below 2^-6.8 (not 2^-9.8) of a row's amax
+  // their last bits: a score is off by at most 2^-14 amax scale sum |k| over those, in a
+  // row whose largest element is 30 times the others some 3e-4 in the mean square, a
+  // tenth of what the bf16 rounding of q itself was.
   static constexpr int COMMON = 3;
   static BST_DEV float load_q(const CtxParams &p, uint8_t *smem, CtxBars *bars, const AttnPiece &pc, int rows, int tid) {
     const bool need16 = !Q8 || pc.t1 > pc.ctx_tiles, need8 = Q8 && pc.t0 < pc.ctx_tiles;
@@ -1400,9 +1402,9 @@ cudaError_t launch_ctx_attn(const AttnWork &w, int d, bool q8, const CtxMaps &ma
   cfg.gridDim = dim3(w.nctas, 1, 1);
   cfg.blockDim = dim3(CT_THREADS, 1, 1);
   // The most rows that a unit of this call can have.  Up to 64, the layout with more
-  // K and V in flight: 8-bit decoding of 16 requests of 512 to 8192 keys 45.5 -> 44.0
-  // us, trees of 16 nodes of 8 such requests 53.5 -> 51.5, 4 requests behind 8192
-  // shared keys 15.1 -> 14.6 (bf16: 21.1 -> 20.6).
+  // K and V in flight (each call on its own, cold L2): 8-bit decoding of 16 requests of
+  // 512 to 8192 keys 58.5 -> 55.8 us, trees of 16 nodes of 8 such requests 65.0 -> 63.0,
+  // 4 requests behind 8192 shared bf16 keys 30.2 -> 29.2.
   const int64_t rows = static_cast<int64_t>(w.prefix_len ? w.B : 1) * w.n_max * w.g;
   auto go = [&](auto d_, auto q8_, auto rm_) {
     constexpr int D = decltype(d_)::value, RM = decltype(rm_)::value;

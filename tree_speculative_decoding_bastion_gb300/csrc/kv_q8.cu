@@ -13,7 +13,7 @@
 // maximum by shuffles, and several rows per lane are in flight at once.
 // Measured (6.7 TB/s is what a copy reaches): 4 prompts of up to 8191 fp32 tokens
 // (8 heads of 128, 228 MB) 50 us, 4.6 TB/s; 16 contexts of up to 8192 read back
-// to bf16 (536 MB) 85.6 us, 6.3 TB/s; one token 3.5 us, 16 accepted paths 6.6 us
+// to bf16 (536 MB) 85.8 us, 6.3 TB/s; one token 3.9 us, 16 accepted paths 6.5 us
 // (dependent loads: counts, page or node, row).
 #include <algorithm>
 
