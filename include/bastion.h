@@ -457,8 +457,8 @@ bastion_status bastion_kv_read_q8(const bastion_kv_cache_q8 *kv, bastion_dtype d
  * off by at most 2^-14 of that below), the softmax weights, times their keys' V
  * scales, as the sum of three e5m2 parts (off by at most 2^-8.8 relative or 2^-24
  * of the row's largest such product, whichever is more; a bf16 weight is off by
- * up to 2^-8); the weights of the tree's own nodes are bf16; accumulation in
- * fp32.  Values may have any size from 2^-90 to 2^100, also side by side: a part
+ * up to 2^-8); the weights of the tree's own nodes are bf16 (and enter the sum
+ * as that); accumulation in fp32.  Values may have any size from 2^-90 to 2^100, also side by side: a part
  * of a result below 2^-70 of the largest |value| among the request's keys, or
  * below 2^-100, may be lost.  dtype f32: fp32 throughout.
  * Requires d in {64, 128}, Hq % Hkv == 0 (any ratio), Hq <= 1024, n_max <= 256,
@@ -483,9 +483,9 @@ bastion_status bastion_tree_attn_q8(const void *q, const void *k_tree, const voi
  * bastion_tree_attn_shared -- bastion_tree_attn for a batch that shares a
  * prefix (prefix, prefix_len as for bastion_tree_attn_q8, both required), with
  * caches of the inputs' type.  Everything else is as for bastion_tree_attn_q8;
- * dtype bf16: softmax weights in bf16, held to at most 2^8 (sums stay finite
- * while keys x the largest |value| is below 2^120; a part of a result below
- * 2^-100 may be lost).
+ * dtype bf16: softmax weights in bf16, divided by the sum of what they were
+ * rounded to, and held to at most 2^8 (sums stay finite while keys x the largest
+ * |value| is below 2^120; a part of a result below 2^-100 may be lost).
  */
 size_t bastion_tree_attn_shared_workspace_size(bastion_dtype dtype, int B, int n_max, int Hq, int Hkv, int d,
                                                const bastion_kv_cache *kv, const bastion_kv_cache *prefix);

@@ -286,3 +286,23 @@ def test_rows_of_q_of_different_sizes(lo, hi, ctx, N, g, d):
     c.call()
     torch.cuda.synchronize()
     check_tight(c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("spread", [0.0, 2.0])
+@pytest.mark.parametrize("rows", [1, 13, 40])
+def test_equal_values_come_out_as_they_are(rows, spread, d):
+    """bf16 caches: where every key holds the same value the result is that value, bit for bit:
+    the weights are divided by the sum of what they were rounded to, and what is left,
+    fp32 sums, is far below half a step of the output."""
+    c = Case(70, [rows, 1], rows, 8, 2, d, "bf16", False, 16, [900, 3], 700, 16, spread=spread)
+    value = torch.randn(2, d, generator=torch.Generator().manual_seed(70)).to(torch.bfloat16).cuda()
+    for cache in (c.own, c.pre):
+        cache.t["v"].copy_(torch.where(torch.isnan(cache.t["v"]), cache.t["v"], value[None, :, None].expand_as(cache.t["v"])))
+    for b, m in enumerate(c.n):
+        c.vt[b, :m] = value
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    for b, m in enumerate(c.n):
+        assert torch.equal(c.out[b, :m], value.repeat_interleave(4, 0)[None].expand(m, -1, -1))

@@ -61,7 +61,7 @@
 // first references); then an 8-bit tile of 128 rows takes 4.9 thousand cycles, bound by the
 // softmax's instructions (issue slots 50% busy, tensor pipe 29%: 4 trees of 128
 // over 32768 keys 531 us), a bf16 one 2.4 thousand (16 trees behind 16381 shared
-// keys 232 us), an 8-bit tile of few rows 1.9 thousand, bound by latency (16 tokens
+// keys 235 us), an 8-bit tile of few rows 1.9 thousand, bound by latency (16 tokens
 // over 512 to 8192 keys 45.5 us, 3.5 TB/s).
 // Every mbarrier wait is bounded in time; after an expiry the CTA issues no
 // further copies, walks its loops to the end with at most two polls a wait and
@@ -334,7 +334,8 @@ struct CtxSoftmax {
   // to their eight bits at any size, so HEAD costs nothing but the last 2^16 of the
   // fp32 range downwards; a weight is at most 2^8, as in the attention over
   // bf16 caches alone, and O stays finite while keys x |V| is below 2^120
-  // (16 trees behind 16381 shared keys: 231 us; HEAD 8 238, HEAD 0 305).
+  // (16 trees behind 16381 shared keys: 231 us; HEAD 8 238, HEAD 0 305, before the
+  // sum took the rounded weights).
   // The 8-bit parts have no such room (SHIFT + TH = 15: the largest weight is then
   // 2^15, an f16).  A larger SHIFT means finer small weights; where the sizes of keys vary
   // as e^(N/2), TH = 4 is exceeded in a quarter of a range's tiles, 7 in an eighth.
@@ -871,12 +872,20 @@ struct CtxSoftmax {
 #pragma unroll
         for (int e = 0; e < C / 2; ++e) {
           float2 v = make_float2(ex2f(x[2 * e]), ex2f(x[2 * e + 1]));
+          if constexpr (!F8) {
+            // bf16 weights: the sum is that of the rounded ones, so that what a weight loses
+            // costs only its share of the differences between the values (error against
+            // 64 bits behind a shared prefix 0.0023 -> 0.0018, where the output's rounding is
+            // 0.0016; 64 single tokens 57 -> 58 us, 16 trees 232 -> 235)
+            w[e] = bf16x2(v.x, v.y);
+            v = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+          }
           l[c / 2 + e] = __fadd2_rn(l[c / 2 + e], v);
           if constexpr (Q8) v = __fmul2_rn(v, w2);
           if constexpr (F8)
             w[e] = weight_pair(v);
-          else
-            w[e] = bf16x2(v.x, v.y);
+          else if constexpr (Q8)
+            w[e] = bf16x2(v.x, v.y);         // (times a power of two: exact)
         }
         if constexpr (F8) {
           // into the 16-byte chunk of the rows in the key's line
