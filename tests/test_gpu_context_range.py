@@ -306,3 +306,32 @@ def test_equal_values_come_out_as_they_are(rows, spread, d):
     assert int(c.err) == 0
     for b, m in enumerate(c.n):
         assert torch.equal(c.out[b, :m], value.repeat_interleave(4, 0)[None].expand(m, -1, -1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [0, 8, 64])
+@pytest.mark.parametrize("shift", [1, 4])
+def test_scales_at_any_address(shift, page, dtype):
+    """Scale bytes need no alignment: the same bits from a copy that begins `shift` bytes on,
+    lengths of every remainder by eight among the requests."""
+    ctx = [1000 + i for i in range(9)]
+    c = Case(71, [2] * 9, 2, 4, 2, 64, dtype, True, page, ctx, 301, page, room=7, v_exp=20)
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    c.check()
+    want = c.out.clone()
+    for cache in (c.own, c.pre):
+        moved = []
+        for name in ("ks", "vs"):
+            t = cache.t[name]
+            room = torch.full((t.numel() + 16,), 254, dtype=torch.uint8, device="cuda")
+            view = room[shift:shift + t.numel()].view(t.shape)
+            view.copy_(t)
+            moved.append(view.view(torch.float8_e8m0fnu))
+        cache.kv = bn.KVQ8(cache.kv.k, cache.kv.v, *moved, cache.kv.block_table)
+    c.out.fill_(5.0)
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    assert torch.equal(c.out, want)
